@@ -102,6 +102,20 @@ def _stream(device: torch.device, stream=None) -> int:
     return stream.cuda_stream
 
 
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream=None) -> torch.Tensor:
+    """An output for a call on `stream` (PyTorch's current one when None), from
+    that stream's memory: a block of the current stream's may still be in use
+    by work that `stream` does not wait for.  The caller goes on with it on the
+    current stream, so that one has to be done with it, too, before the
+    allocator hands it out again."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _on_device(fn):
     """Run the call with its first tensor's GPU as the current device, so that
     the library sizes its launches for that device and launches there (the

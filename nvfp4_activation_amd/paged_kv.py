@@ -11,6 +11,10 @@ what each computes and how a record is laid out.  A step of a server:
 one); its page size follows from the head dimension of k or q.  ``amax`` holds
 the maxima of rotated K and V that fix the two global scales, for instance
 from ``rotamax`` on a calibration tensor.
+
+A call runs on PyTorch's current stream, or on ``stream``; what it allocates is
+memory of that stream, and waiting for it before using the outputs elsewhere
+is the caller's part.
 """
 from __future__ import annotations
 
@@ -20,7 +24,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _buf, _check, _p, _ptr, lib
+from . import _buf, _check, _empty, _p, _ptr, lib
 
 __all__ = ["KvPlan", "kv_append", "kv_attention", "kv_attention_workspace", "kv_cache", "kv_page_bytes", "kv_plan"]
 
@@ -182,8 +186,8 @@ def kv_plan(cached: torch.Tensor, added: torch.Tensor, table: torch.Tensor, free
     _within(page_size, _MOST32, "page_size")
     _within(tokens, _MOST32, "tokens")
     if out is None:
-        ints = torch.empty(2 * n + 4, dtype=torch.int32, device=device).split((n + 1, n, 1, 2))
-        out = KvPlan(torch.empty(tokens, dtype=torch.int64, device=device), *ints)
+        ints = _empty(2 * n + 4, torch.int32, device, stream).split((n + 1, n, 1, 2))
+        out = KvPlan(_empty(tokens, torch.int64, device, stream), *ints)
     else:
         _buf(out[0], tokens, torch.int64, device, "slots")
         for t, size, name in zip(out[1:], (n + 1, n, 1, 2), KvPlan._fields[1:]):
@@ -262,7 +266,7 @@ def kv_attention(q: torch.Tensor, cache: torch.Tensor, amax: torch.Tensor, table
     qs = _rows(q, "q")
     c, b = _batch_arg(q, cache, amax, table, cu_q, kv_lens, max_q, max_kv, causal, window, scale, rotate)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _empty(q.shape, q.dtype, q.device, stream)
         os_ = _strides2(q.shape[1] * q.shape[2], q.shape[2])
     else:
         os_ = _rows(out, "out", q.dtype, q.device)
