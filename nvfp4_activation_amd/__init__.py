@@ -188,7 +188,7 @@ def rotamax(x: torch.Tensor, rotate: bool = True, amax: torch.Tensor | None = No
     """Pass 1: the rotated global amax, as a float32 device tensor [1]."""
     rows, cols = _check_input(x)
     if amax is None:
-        amax = torch.empty(1, dtype=torch.float32, device=x.device)
+        amax = _empty(1, torch.float32, x.device, stream)
     _buf(amax, 1, torch.float32, x.device, "amax")
     fn = _variant(x, "nvfp4_rotamax")
     _check(fn, getattr(lib, fn)(_ptr(x), rows, cols, int(bool(rotate)), _ptr(amax),
@@ -203,9 +203,9 @@ def quant_from_amax(x: torch.Tensor, amax: torch.Tensor, rotate: bool = True,
     Returns (q uint8 [rows, cols/2], s uint8 [rows, cols/16], g float32 [1])."""
     rows, cols = _check_input(x)
     if out is None:
-        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
-        s = torch.empty(rows, cols // 16, dtype=torch.uint8, device=x.device)
-        g = torch.empty(1, dtype=torch.float32, device=x.device)
+        q = _empty((rows, cols // 2), torch.uint8, x.device, stream)
+        s = _empty((rows, cols // 16), torch.uint8, x.device, stream)
+        g = _empty(1, torch.float32, x.device, stream)
     else:
         q, s, g = out
     _buf(amax, 1, torch.float32, x.device, "amax")
@@ -225,10 +225,10 @@ def rotquant(x: torch.Tensor, rotate: bool = True, out: tuple | None = None, str
     g float32 [1] global scale, amax float32 [1])."""
     rows, cols = _check_input(x)
     if out is None:
-        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
-        s = torch.empty(rows, cols // 16, dtype=torch.uint8, device=x.device)
-        g = torch.empty(1, dtype=torch.float32, device=x.device)
-        a = torch.empty(1, dtype=torch.float32, device=x.device)
+        q = _empty((rows, cols // 2), torch.uint8, x.device, stream)
+        s = _empty((rows, cols // 16), torch.uint8, x.device, stream)
+        g = _empty(1, torch.float32, x.device, stream)
+        a = _empty(1, torch.float32, x.device, stream)
     else:
         q, s, g, a = out
     _check_out4(x, rows, cols, q, s, g, a, rows * cols // 16)
@@ -247,10 +247,10 @@ def rotquant_timed(x: torch.Tensor, events: list, rotate: bool = True, out: tupl
     kernels launched)."""
     rows, cols = _check_input(x)
     if out is None:
-        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
-        s = torch.empty(rows, cols // 16, dtype=torch.uint8, device=x.device)
-        g = torch.empty(1, dtype=torch.float32, device=x.device)
-        a = torch.empty(1, dtype=torch.float32, device=x.device)
+        q = _empty((rows, cols // 2), torch.uint8, x.device, stream)
+        s = _empty((rows, cols // 16), torch.uint8, x.device, stream)
+        g = _empty(1, torch.float32, x.device, stream)
+        a = _empty(1, torch.float32, x.device, stream)
     else:
         q, s, g, a = out
     _check_out4(x, rows, cols, q, s, g, a, rows * cols // 16)
@@ -277,7 +277,7 @@ def dequant(q: torch.Tensor, s: torch.Tensor, g: torch.Tensor, rotate: bool = Tr
         raise ValueError("q and s shapes disagree")
     _decode_inputs(q, s, g, s.numel())
     if out is None:
-        out = torch.empty(rows, cols, dtype=torch.float32, device=q.device)
+        out = _empty((rows, cols), torch.float32, q.device, stream)
     _buf(out, rows * cols, torch.float32, q.device, "out")
     _check("nvfp4_dequant", lib.nvfp4_dequant(_ptr(q), _ptr(s), _ptr(g), rows, cols,
                                               int(bool(rotate)), _ptr(out),
@@ -298,10 +298,10 @@ def rotquant_swizzled(x: torch.Tensor, rotate: bool = True, out: tuple | None = 
     Returns (q uint8 [rows, cols/2], s uint8 [swizzled_scale_bytes], g, amax)."""
     rows, cols = _check_input(x)
     if out is None:
-        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
-        s = torch.empty(swizzled_scale_bytes(rows, cols), dtype=torch.uint8, device=x.device)
-        g = torch.empty(1, dtype=torch.float32, device=x.device)
-        a = torch.empty(1, dtype=torch.float32, device=x.device)
+        q = _empty((rows, cols // 2), torch.uint8, x.device, stream)
+        s = _empty(swizzled_scale_bytes(rows, cols), torch.uint8, x.device, stream)
+        g = _empty(1, torch.float32, x.device, stream)
+        a = _empty(1, torch.float32, x.device, stream)
     else:
         q, s, g, a = out
     _check_out4(x, rows, cols, q, s, g, a, swizzled_scale_bytes(rows, cols))
@@ -319,7 +319,7 @@ def dequant_swizzled(q: torch.Tensor, s: torch.Tensor, g: torch.Tensor, rotate: 
     rows, cols = q.shape[0], q.shape[1] * 2
     _decode_inputs(q, s, g, swizzled_scale_bytes(rows, cols))
     if out is None:
-        out = torch.empty(rows, cols, dtype=torch.float32, device=q.device)
+        out = _empty((rows, cols), torch.float32, q.device, stream)
     _buf(out, rows * cols, torch.float32, q.device, "out")
     _check("nvfp4_dequant_swizzled", lib.nvfp4_dequant_swizzled(
         _ptr(q), _ptr(s), _ptr(g), rows, cols, int(bool(rotate)), _ptr(out),
@@ -332,7 +332,7 @@ def rotate16(x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> t
     """The block rotation alone: float32 [rows, cols] = x H16 per 16-element block."""
     rows, cols = _check_input(x)
     if out is None:
-        out = torch.empty(rows, cols, dtype=torch.float32, device=x.device)
+        out = _empty((rows, cols), torch.float32, x.device, stream)
     _buf(out, rows * cols, torch.float32, x.device, "out")
     fn = _variant(x, "nvfp4_rotate16")
     _check(fn, getattr(lib, fn)(_ptr(x), rows, cols, _ptr(out), _stream(x.device, stream)))
@@ -347,7 +347,7 @@ def rotate_matrix(x: torch.Tensor, r: torch.Tensor, out: torch.Tensor | None = N
     rows, cols = _check_input(x)
     _buf(r, 256, torch.float32, x.device, "r")
     if out is None:
-        out = torch.empty(rows, cols, dtype=torch.float32, device=x.device)
+        out = _empty((rows, cols), torch.float32, x.device, stream)
     _buf(out, rows * cols, torch.float32, x.device, "out")
     fn = _variant(x, "nvfp4_rotate_matrix")
     _check(fn, getattr(lib, fn)(_ptr(x), rows, cols, _ptr(r), _ptr(out),
@@ -361,8 +361,8 @@ def mx_rotquant(x: torch.Tensor, rotate: bool = True, out: tuple | None = None, 
     Returns (q uint8 [rows, cols/2], s uint8 [rows, cols/32] E8M0 bytes)."""
     rows, cols = _check_input(x, 32)
     if out is None:
-        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
-        s = torch.empty(rows, cols // 32, dtype=torch.uint8, device=x.device)
+        q = _empty((rows, cols // 2), torch.uint8, x.device, stream)
+        s = _empty((rows, cols // 32), torch.uint8, x.device, stream)
     else:
         q, s = out
     _buf(q, rows * cols // 2, torch.uint8, x.device, "q")
@@ -383,7 +383,7 @@ def mx_dequant(q: torch.Tensor, s: torch.Tensor, rotate: bool = True,
         raise ValueError("q and s shapes disagree")
     _decode_inputs(q, s, None, s.numel())
     if out is None:
-        out = torch.empty(rows, cols, dtype=torch.float32, device=q.device)
+        out = _empty((rows, cols), torch.float32, q.device, stream)
     _buf(out, rows * cols, torch.float32, q.device, "out")
     _check("mxfp4_dequant", lib.mxfp4_dequant(_ptr(q), _ptr(s), rows, cols, int(bool(rotate)),
                                               _ptr(out), _stream(q.device, stream)))
@@ -409,8 +409,8 @@ def stream_calibrate_single(x: torch.Tensor, out: tuple | None = None, stream=No
 def _calibrate(name: str, x: torch.Tensor, out, stream):
     rows, cols = _check_input(x)
     if out is None:
-        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
-        s = torch.empty(rows, cols // 16, dtype=torch.uint8, device=x.device)
+        q = _empty((rows, cols // 2), torch.uint8, x.device, stream)
+        s = _empty((rows, cols // 16), torch.uint8, x.device, stream)
     else:
         q, s = out
     _buf(q, rows * cols // 2, torch.uint8, x.device, "q")

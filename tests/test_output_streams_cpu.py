@@ -72,7 +72,29 @@ def kv_attention(**kw):
                            dev(1, dtype=torch.int32), **kw)
 
 
-CALLS = [kv_plan, kv_attention]
+def named(name, *args):
+    def call(**kw):
+        return getattr(nv, name)(*args, **kw)
+    call.__name__ = name
+    return call
+
+
+class Event:
+    cuda_event = 1
+
+
+u8 = torch.uint8
+CALLS = [kv_plan, kv_attention] + [
+    named(name, dev(4, 64)) for name in ("rotamax", "rotquant", "rotquant_swizzled", "rotate16", "mx_rotquant",
+                                         "stream_calibrate", "stream_calibrate_single")
+] + [
+    named("quant_from_amax", dev(4, 64), dev(1)),
+    named("rotquant_timed", dev(4, 64), [Event(), Event()]),
+    named("rotate_matrix", dev(4, 64), dev(16, 16)),
+    named("dequant", dev(4, 32, dtype=u8), dev(4, 4, dtype=u8), dev(1)),
+    named("dequant_swizzled", dev(4, 32, dtype=u8), dev(512, dtype=u8), dev(1)),
+    named("mx_dequant", dev(4, 32, dtype=u8), dev(4, 2, dtype=u8)),
+]
 
 
 @pytest.mark.parametrize("call", CALLS, ids=lambda c: c.__name__)

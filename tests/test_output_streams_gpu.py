@@ -50,7 +50,31 @@ def kv_attention(nv, stream=None, tokens=3):
     return nv.kv_attention(q, *args, stream=stream)
 
 
-CALLS = [kv_plan, kv_attention]
+def rows():
+    x = torch.randn(64, 256, device=DEV, generator=torch.Generator(DEV).manual_seed(3))
+    torch.cuda.synchronize()
+    return x
+
+
+def named(name, make):
+    def call(nv, **kw):
+        args = make(nv)
+        torch.cuda.synchronize()
+        return getattr(nv, name)(*args, **kw)
+    call.__name__ = name
+    return call
+
+
+CALLS = [kv_plan, kv_attention] + [
+    named(name, lambda nv: (rows(),)) for name in ("rotamax", "rotquant", "rotquant_swizzled", "rotate16",
+                                                   "mx_rotquant")
+] + [
+    named("quant_from_amax", lambda nv: (rows(), nv.rotamax(rows()))),
+    named("rotate_matrix", lambda nv: (rows(), torch.eye(16, device=DEV))),
+    named("dequant", lambda nv: nv.rotquant(rows())[:3]),
+    named("dequant_swizzled", lambda nv: nv.rotquant_swizzled(rows())[:3]),
+    named("mx_dequant", lambda nv: nv.mx_rotquant(rows())),
+]
 
 
 @pytest.mark.parametrize("call", CALLS, ids=lambda c: c.__name__)
