@@ -373,8 +373,9 @@ int64_t nvfp4_kv_page_bytes(int32_t page_size, int32_t head_dim);
  * p % page_size, or -1 where that entry is negative or past the width.
  *   cached, added  device, int32 [requests]; negative lengths count as 0, and
  *                  the sums are to stay below 2^31.
- *   table          device, int32 [requests, table_width], updated in place:
- *                  calling again with the same head writes the same.
+ *   table          device, int32 [requests, table_width], at most 2^60 entries,
+ *                  updated in place: calling again with the same head writes
+ *                  the same.
  *   free_pages     device, int32 [free_count]; head_in (device, 1 int32) is
  *                  the first entry not yet taken (a negative one counts as
  *                  0), head_out (device, 1 int32) receives the next such
@@ -429,9 +430,10 @@ nvfp4_status nvfp4_kv_append_f32(const float *k, const float *v, int64_t tokens,
  * when window > 0.  Query head h reads key head h / (q_heads / kv_heads).
  * out = sum_j softmax_j(scale q.k_j) v_j; a query that sees no key gives 0;
  * rows of q in no request are left as they were in out.
- *   table      device, int32 [requests, table_width].  A query that sees a key
- *              past the row's width, or on a page whose id is outside
- *              [0, pages), is NaN; entries that no query sees are not used.
+ *   table      device, int32 [requests, table_width], at most 2^60 entries.  A
+ *              query that sees a key past the row's width, or on a page whose
+ *              id is outside [0, pages), is NaN; entries that no query sees
+ *              are not used.
  *   cu_q       device, int32 [requests + 1], not decreasing, within
  *              [0, tokens].
  *   kv_lens    device, int32 [requests], at most 2^31 - 2^16; negative counts

@@ -24,6 +24,9 @@ int log2_of(int64_t v) {
   return s;
 }
 
+// A block table of more entries would have a size that 64 bits do not hold.
+bool table_fits(int64_t requests, int64_t width) { return width == 0 || requests <= (int64_t{1} << 60) / width; }
+
 bool page_size_ok(int64_t p) { return p >= 16 && p <= 65536 && (p & (p - 1)) == 0; }
 bool head_dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }
 
@@ -68,7 +71,8 @@ nvfp4_status check_rows(int64_t tokens, int32_t heads, int32_t dim, const int64_
   if (ts < 0 || hs < 0) return NVFP4_ERR_SHAPE;
   const int64_t most = int64_t{1} << 60;
   if ((tokens > 1 && ts > most / tokens / size) || (heads > 1 && hs > most / heads / size)) return NVFP4_ERR_SHAPE;
-  if ((ts * size) % 16 != 0 || (hs * size) % 16 != 0 || !kv_aligned(p, 16)) return NVFP4_ERR_ALIGN;
+  // a stride that its count does not use may be any: no product of it is formed
+  if (ts % (16 / size) != 0 || hs % (16 / size) != 0 || !kv_aligned(p, 16)) return NVFP4_ERR_ALIGN;
   *span = span_of(p, tokens == 0 ? 0 : ((tokens - 1) * ts + (heads - 1) * hs + dim) * size);
   return NVFP4_OK;
 }
@@ -80,7 +84,8 @@ nvfp4_status plan(const int32_t* cached, const int32_t* added, int64_t requests,
                   int64_t* slots, int64_t max_tokens, int32_t* cu_q, int32_t* kv_lens, int32_t* head_out,
                   int32_t* missing, hipStream_t st) {
   if (requests < 0 || requests > INT32_MAX || width < 0 || width > INT32_MAX || free_count < 0 ||
-      free_count > INT32_MAX || max_tokens < 0 || max_tokens > INT32_MAX || !page_size_ok(page_size))
+      free_count > INT32_MAX || max_tokens < 0 || max_tokens > INT32_MAX || !page_size_ok(page_size) ||
+      !table_fits(requests, width))
     return NVFP4_ERR_SHAPE;
   const bool has_table = requests != 0 && width != 0;
   if ((requests != 0 && (!cached || !added || !kv_lens)) || (has_table && !table) || (free_count != 0 && !free_pages) ||
@@ -192,7 +197,8 @@ nvfp4_status plan_attention(int64_t tokens, int32_t q_heads, const nvfp4_kv_cach
   if (st != NVFP4_OK) return st;
   if (!b) return NVFP4_ERR_NULL;
   if (q_heads < 1 || q_heads % c->kv_heads != 0 || tokens < 0 || tokens > INT32_MAX / q_heads || b->requests < 0 ||
-      b->requests > INT32_MAX - 1 || b->table_width < 0 || b->table_width > INT32_MAX || b->max_q < 0 || b->max_kv < 0)
+      b->requests > INT32_MAX - 1 || b->table_width < 0 || b->table_width > INT32_MAX ||
+      !table_fits(b->requests, b->table_width) || b->max_q < 0 || b->max_kv < 0)
     return NVFP4_ERR_SHAPE;
   const int64_t group = q_heads / c->kv_heads, cus = kv_device_cus();
   int64_t max_q = b->max_q < tokens ? b->max_q : tokens;
