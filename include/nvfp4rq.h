@@ -457,7 +457,8 @@ typedef struct nvfp4_kv_batch {
 /*
  *   q, out     device, [tokens, q_heads, head_dim], 16-byte aligned, strided
  *              as k above (q_strides, out_strides); q_heads a multiple of
- *              kv_heads.  out may not overlap q or the cache.
+ *              kv_heads, tokens * q_heads at most 2^31 - 2^16.  out may not
+ *              overlap q or the cache.
  *   workspace  device, at least nvfp4_kv_attention_workspace bytes, 16-byte
  *              aligned (NULL when that is 0); holds partial sums during the
  *              call.  Calls that share one must be ordered.

@@ -222,6 +222,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 // ---------------------------------------------------------------- a request
 
 constexpr int kMostKeys = INT32_MAX - 65535;  // key arithmetic past the last tile stays in 32 bits
+constexpr int kMostRows = INT32_MAX - 65535;  // tokens * query heads: a unit's first row past the last one, too
 struct Request {
   int row0, n, kv;  // first row of q, queries, keys
 };
@@ -429,7 +430,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, rows_waves(sizeof(T) == 4, D, RT))
   const int shift = a.cache.shift, heads = a.cache.kv_heads;
   const int64_t record = Rec::bytes(shift);
   auto query_of = [&](int row) { return static_cast<int>(a.by_group.div(static_cast<uint32_t>(row))); };
-  auto rows_of = [&](const Request& q) {  // below 2^31: tokens * query heads is
+  auto rows_of = [&](const Request& q) {  // at most kMostRows: tokens * query heads is
     const int rows = q.n * a.group;
     return rows > a.few ? 0 : rows;
   };

@@ -196,7 +196,7 @@ nvfp4_status plan_attention(int64_t tokens, int32_t q_heads, const nvfp4_kv_cach
   const nvfp4_status st = check_cache_shape(c);
   if (st != NVFP4_OK) return st;
   if (!b) return NVFP4_ERR_NULL;
-  if (q_heads < 1 || q_heads % c->kv_heads != 0 || tokens < 0 || tokens > INT32_MAX / q_heads || b->requests < 0 ||
+  if (q_heads < 1 || q_heads % c->kv_heads != 0 || tokens < 0 || tokens > kMostRows / q_heads || b->requests < 0 ||
       b->requests > INT32_MAX - 1 || b->table_width < 0 || b->table_width > INT32_MAX ||
       !table_fits(b->requests, b->table_width) || b->max_q < 0 || b->max_kv < 0)
     return NVFP4_ERR_SHAPE;

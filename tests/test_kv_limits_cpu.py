@@ -2,10 +2,13 @@
 CPU."""
 from __future__ import annotations
 
+import ctypes
+import itertools
 import os
 
 import pytest
 
+from test_kv_cpu import batch, cache, lib
 from test_kv_host_cpu import CSRC, FLAGS, HELPERS, INC, ROCM, hipcc, run
 
 needs_hipcc = pytest.mark.skipif(not os.path.exists(os.path.join(ROCM, "bin", "hipcc")), reason="hipcc not installed")
@@ -35,3 +38,18 @@ def test_extremes_under_asan_ubsan(tmp_path):
         pytest.skip("a GPU is visible; the driver only runs without one")
     assert r.returncode == 0, r.stdout + r.stderr
     assert "clean" in r.stdout
+
+
+def test_most_rows():
+    """Row numbers are 32-bit and counted in steps of a unit, also past the
+    last one: tokens * query heads is at most 2^31 - 2^16, whatever the
+    estimates."""
+    top = (1 << 31) - (1 << 16)
+    for heads, d, max_q in itertools.product((1, 8, 24, 128), (64, 128, 256), (0, 1)):
+        def need(tokens):
+            return lib.nvfp4_kv_attention_workspace(
+                tokens, heads, ctypes.byref(cache(kv_heads=1, head_dim=d)), ctypes.byref(batch(requests=1, max_q=max_q)))
+
+        assert need(top // heads) >= 0
+        assert need(top // heads + 1) == -1
+        assert need(((1 << 31) - 1) // heads) == -1
