@@ -208,6 +208,30 @@ __device__ __forceinline__ int row_exponent(float top) {
   return 12 - (__builtin_amdgcn_frexp_expf(top) - 1);
 }
 
+// The factor of a row's products in the log2 domain, scale log2(e) g 2^-e.
+// Significands and exponents apart: however small g or the scale, what the
+// other or the query's 2^e makes up for keeps its bits.  Not 0, so that a
+// masked logit stays -inf (|s| < 2^34: nothing is lost), and not infinite, so
+// that a logit of 0 stays 0.
+__device__ __forceinline__ float logit_factor(float scale, float amax, int e) {
+  const float g = global_scale(amax);
+  const float f = __builtin_amdgcn_frexp_mantf(scale) * kLog2e * __builtin_amdgcn_frexp_mantf(g);
+  const int x = __builtin_amdgcn_frexp_expf(scale) + __builtin_amdgcn_frexp_expf(g) - e;
+  return __builtin_amdgcn_fmed3f(__builtin_ldexpf(f, x), 0x1p-126f, 0x1.fffffep127f);
+}
+
+// What brings a row's sums to its result, g / l: where g is so small that the
+// quotient may be subnormal (l < 2^46), times 2^100, with `back` to take that
+// off the result, exactly, after everything else.  0 for a row without keys.
+struct OutScale {
+  float f, back;
+};
+__device__ __forceinline__ OutScale out_scale(float amax, float l) {
+  const float g = global_scale(amax);
+  const bool small = g < 0x1p-60f;  // the same for every row
+  return OutScale{l == 0.0f ? 0.0f : (small ? g * 0x1p100f : g) / l, small ? 0x1p-100f : 1.0f};
+}
+
 // Inclusive sum over the wave.
 __device__ __forceinline__ int wave_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
@@ -331,12 +355,16 @@ __device__ __forceinline__ bool deal_out(const AttnArgs<T>& a, int n, F tiles, i
 // Scales a block of an output row, rotates it back and writes it.
 template <typename T>
 __device__ __forceinline__ void write_block(const AttnArgs<T>& a, int row0, int head, int row, int block,
-                                            float z[16], float f) {
+                                            float z[16], OutScale f) {
   const int oi = static_cast<int>(a.by_group.div(static_cast<uint32_t>(row)));
   const int oh = head * a.group + (row - oi * a.group);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] *= f;
+  for (int i = 0; i < 16; ++i) z[i] *= f.f;
   if (a.cache.rotate) rotate16_block(z);
+  if (f.back != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] *= f.back;
+  }
   store16(a.out + static_cast<int64_t>(row0 + oi) * a.o_token + oh * a.o_head + block * 16, z);
 }
 
@@ -637,8 +665,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, rows_waves(sizeof(T) == 4, D, RT))
           qf[rt][0][k][j] = h;
           if (kSplit) qf[rt][NQ - 1][k][j] = static_cast<_Float16>(v - static_cast<float>(h));
         }
-      // not 0, so that a masked logit stays -inf: |s| < 2^34, so nothing is lost
-      c[rt] = __builtin_fmaxf(__builtin_ldexpf(a.scale * kLog2e * global_scale(a.cache.amax[0]), -e), 0x1p-126f);
+      c[rt] = logit_factor(a.scale, a.cache.amax[0], e);
       const int64_t pos = static_cast<int64_t>(rq.kv) - rq.n + qi;
       see_lo[rt] = 0;
       see_hi[rt] = rq.kv;
@@ -816,7 +843,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, rows_waves(sizeof(T) == 4, D, RT))
             a.part[a.part_ml + 2 * slot + 1] = ll;
           }
         } else {
-          write_block(a, rq.row0, head, orow, b, z, ll == 0.0f ? 0.0f : global_scale(a.cache.amax[1]) / ll);
+          write_block(a, rq.row0, head, orow, b, z, out_scale(a.cache.amax[1], ll));
         }
       }
       __syncthreads();  // the next rows write the merge buffers again
@@ -1047,7 +1074,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_tiles_kernel(AttnArgs
           qf[0][b][i] = h;
           if (kSplit) qf[NQ - 1][b][i] = static_cast<_Float16>(v - static_cast<float>(h));
         }
-      c = __builtin_fmaxf(__builtin_ldexpf(a.scale * kLog2e * global_scale(a.cache.amax[0]), -e), 0x1p-126f);
+      c = logit_factor(a.scale, a.cache.amax[0], e);
     }
     const int64_t pos = static_cast<int64_t>(rq.kv) - rq.n + qi;
     int see_lo = 0, see_hi = rq.kv;
@@ -1317,7 +1344,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_tiles_kernel(AttnArgs
         a.part[a.part_ml + 2 * slot] = m;
         a.part[a.part_ml + 2 * slot + 1] = l;
       }
-      const float f = l == 0.0f ? 0.0f : global_scale(a.cache.amax[1]) / l;
+      const OutScale f = out_scale(a.cache.amax[1], l);
       // element 8 c + j, c = 8 ga + 4 half + b, is in o[j / JW][4 (ga + GA (j % JW)) + b]
 #pragma unroll
       for (int ga = 0; ga < Sh::GA; ++ga)
@@ -1382,7 +1409,6 @@ __device__ __forceinline__ void join_row(const AttnArgs<T>& a, const JoinPart& p
   float z[16], ll = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-  const float gv = global_scale(a.cache.amax[1]);
   for (int s = s0; s < n; s += 32) {
     if (s != s0) fetch(s);
 #pragma unroll
@@ -1405,7 +1431,7 @@ __device__ __forceinline__ void join_row(const AttnArgs<T>& a, const JoinPart& p
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] += __shfl_xor(z[i], d);
   }
-  if (s0 == 0) write_block(a, row0, head, row, b, z, ll == 0.0f ? 0.0f : gv / ll);
+  if (s0 == 0) write_block(a, row0, head, row, b, z, out_scale(a.cache.amax[1], ll));
 }
 
 // Workgroups (w, .) join the unit that workgroup w's range of tiles begins
@@ -1428,7 +1454,6 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs<T> a, JoinPa
   if (n <= 4) {
     // a lane a block of a row, which sums its parts by itself
     constexpr int L = D / 16;
-    const float gv = global_scale(a.cache.amax[1]);
     const float2* ml = reinterpret_cast<const float2*>(p.part + p.part_ml);
     for (int i = 256 * blockIdx.y + threadIdx.x; i < count * L; i += 256 * gridDim.y) {
       const int r = i / L, b = i % L;
@@ -1461,7 +1486,7 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs<T> a, JoinPa
           z[4 * k + 3] = __builtin_fmaf(f, v[s][k].w, z[4 * k + 3]);
         }
       }
-      write_block(a, u.row0, u.head, u.base + r, b, z, ll == 0.0f ? 0.0f : gv / ll);
+      write_block(a, u.row0, u.head, u.base + r, b, z, out_scale(a.cache.amax[1], ll));
     }
     return;
   }
