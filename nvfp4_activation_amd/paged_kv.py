@@ -218,6 +218,19 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torc
     return cache
 
 
+class _NoGradient(torch.autograd.Function):
+    """The result of a call on x that has no backward pass, kept in x's graph so
+    that one through it is refused rather than lost."""
+
+    @staticmethod
+    def forward(ctx, x, call):
+        return call()
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("kv_attention has no backward pass: call it on q.detach() or under torch.no_grad()")
+
+
 def _batch_arg(q, cache, amax, table, cu_q, kv_lens, max_q, max_kv, causal, window, scale, rotate):
     device = q.device
     c = _cache_arg(cache, amax, _within(q.shape[1], _MOST32, "q's heads"), q.shape[2], rotate, device)
@@ -262,7 +275,13 @@ def kv_attention(q: torch.Tensor, cache: torch.Tensor, amax: torch.Tensor, table
     (bounds from the shapes when None); they shape the launch, not the result.
     scale: head_dim ** -0.5 when None.  Rows in no request are left as they were
     in out.  workspace: a uint8 tensor of kv_attention_workspace bytes, allocated
-    when None; calls that share one must be ordered.  No gradients."""
+    when None; calls that share one must be ordered.  No gradients: a backward
+    pass that reaches the result raises, unless it was written to the caller's
+    out, which keeps no record of q."""
+    if out is None and torch.is_grad_enabled() and isinstance(q, torch.Tensor) and q.requires_grad:
+        return _NoGradient.apply(q, lambda: kv_attention(
+            q.detach(), cache, amax, table, cu_q, kv_lens, max_q, max_kv, causal, window, scale, rotate, None,
+            workspace, stream))
     qs = _rows(q, "q")
     c, b = _batch_arg(q, cache, amax, table, cu_q, kv_lens, max_q, max_kv, causal, window, scale, rotate)
     if out is None:

@@ -116,3 +116,15 @@ def test_nothing_is_recorded_on_the_current_stream_alone(allocations, call, monk
     monkeypatch.setattr(paged_kv, "_stream", lambda device, stream=None: 0)
     call()
     assert made and all(on is None for on, _ in made) and not recorded
+
+
+def test_a_backward_pass_through_the_attention_is_refused(allocations):
+    q = dev(3, 4, 64).requires_grad_()
+    cache = dev(4, 2, 16 * 64 * 9 // 8, dtype=torch.uint8)
+    rest = (cache, dev(2), dev(1, 3, dtype=torch.int32), dev(2, dtype=torch.int32), dev(1, dtype=torch.int32))
+    got = nv.kv_attention(q, *rest, stream=Stream())
+    assert got.requires_grad
+    with pytest.raises(RuntimeError, match="no backward pass"):
+        got.sum().backward()
+    with torch.no_grad():
+        assert not nv.kv_attention(q, *rest, stream=Stream()).requires_grad
