@@ -53,3 +53,17 @@ def test_most_rows():
         assert need(top // heads) >= 0
         assert need(top // heads + 1) == -1
         assert need(((1 << 31) - 1) // heads) == -1
+
+
+@pytest.mark.skipif(not os.path.exists(os.path.join(ROCM, "include", "hip", "hip_runtime.h")),
+                    reason="the HIP headers are not installed")
+def test_division_by_launch_constants(tmp_path):
+    """FastDiv's own code, compiled for the host: quotients around multiples of
+    some 470,000 divisors."""
+    exe = tmp_path / "kv_fastdiv"
+    r = run(["g++", "-std=c++17", "-O2", "-Wall", "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", f"-I{INC}",
+             f"-I{CSRC}", os.path.join(HELPERS, "kv_fastdiv.cpp"), "-o", exe])
+    assert r.returncode == 0, r.stdout + r.stderr
+    r = run([exe], timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert int(r.stdout.split()[0]) > 10 ** 7
