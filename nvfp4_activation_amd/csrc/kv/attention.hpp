@@ -61,6 +61,7 @@ struct AttnArgs {
   KvView cache;
   const int32_t *table, *cu_q, *kv_lens;
   int64_t table_width;
+  int32_t reach;                    // keys that a row of the table has room for, kMostKeys at most
   int32_t tokens, requests, group;  // group: query heads per key head
   int32_t causal, window;
   float scale;
@@ -260,13 +261,15 @@ __device__ __forceinline__ Request request_of(const AttnArgs<T>& a, int r) {
 }
 
 // Keys [lo, hi) that any of the queries [i0, i1) of a request sees; empty when
-// hi <= lo.
+// hi <= lo.  Those past the table's row are left out, so that a length too
+// large costs no time: a query that sees one is NaN whatever the others hold
+// (see_of).
 struct Keys {
   int lo, hi;
 };
 template <typename T>
 __device__ __forceinline__ Keys keys_of(const AttnArgs<T>& a, const Request& r, int i0, int i1) {
-  Keys k{0, r.kv};
+  Keys k{0, r.kv < a.reach ? r.kv : a.reach};
   if (a.causal) {
     const int64_t last = static_cast<int64_t>(r.kv) - r.n + i1 - 1;
     if (last + 1 < k.hi) k.hi = last < -1 ? 0 : static_cast<int>(last + 1);
@@ -275,6 +278,19 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs<T>& a, const Request& r, 
     const int64_t first = static_cast<int64_t>(r.kv) - r.n + i0 - a.window + 1;
     if (first > 0) k.lo = first > k.hi ? k.hi : static_cast<int>(first);
   }
+  return k;
+}
+
+// Keys [lo, hi) of query i among those of keys_of; NaN in *sum, the row's sum
+// of weights to begin with, where it sees others past them, else 0.
+template <typename T>
+__device__ __forceinline__ Keys see_of(const AttnArgs<T>& a, const Request& r, int i, float* sum) {
+  const int64_t pos = static_cast<int64_t>(r.kv) - r.n + i;
+  Keys k{0, r.kv};
+  if (a.causal && pos + 1 < r.kv) k.hi = pos < 0 ? 0 : static_cast<int>(pos + 1);
+  if (a.window && pos - a.window + 1 > 0) k.lo = static_cast<int>(pos - a.window + 1);
+  *sum = k.hi > a.reach && k.hi > k.lo ? NAN : 0.0f;
+  if (k.hi > a.reach) k.hi = a.reach;
   return k;
 }
 
@@ -563,7 +579,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, rows_waves(sizeof(T) == 4, D, RT))
       const int key = (t_first + kAttnWaves * (b + (lane >> 1))) * kTile + 16 * (lane & 1);
       const int64_t col = key >> shift;
       int p = -1;
-      if (key < t_end * kTile && key < keys.hi && key + 16 > keys.lo && col < a.table_width) p = row_table[col];
+      if (key < t_end * kTile && key < keys.hi && key + 16 > keys.lo) p = row_table[col];
       return p >= 0 && p < a.cache.pages ? p : -1;
     };
     int pages = lookup(0), pages_at = 0;
@@ -645,6 +661,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, rows_waves(sizeof(T) == 4, D, RT))
     half8_t qf[RT][NQ][KK];
     float c[RT];                  // logit factors, log2 domain
     int see_lo[RT], see_hi[RT];   // keys that the row sees
+    float m[RT], l[RT];           // maximum and sum of its weights
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int row = base + 16 * rt + r16;
@@ -666,21 +683,17 @@ __global__ __launch_bounds__(64 * kAttnWaves, rows_waves(sizeof(T) == 4, D, RT))
           if (kSplit) qf[rt][NQ - 1][k][j] = static_cast<_Float16>(v - static_cast<float>(h));
         }
       c[rt] = logit_factor(a.scale, a.cache.amax[0], e);
-      const int64_t pos = static_cast<int64_t>(rq.kv) - rq.n + qi;
-      see_lo[rt] = 0;
-      see_hi[rt] = rq.kv;
-      if (a.causal && pos + 1 < rq.kv) see_hi[rt] = pos < 0 ? 0 : static_cast<int>(pos + 1);
-      if (a.window && pos - a.window + 1 > 0) see_lo[rt] = static_cast<int>(pos - a.window + 1);
+      const Keys see = see_of(a, rq, qi, &l[rt]);
+      see_lo[rt] = see.lo;
+      see_hi[rt] = see.hi;
     }
     // keys that every row sees
     const Keys inner{a.window ? keys_of(a, rq, i1 - 1, i1).lo : 0, keys_of(a, rq, i0, i0 + 1).hi};
 
-    float m[RT], l[RT];
     f32x4 o[RT][L];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       m[rt] = -INFINITY;
-      l[rt] = 0.0f;
 #pragma unroll
       for (int j = 0; j < L; ++j) o[rt][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -1076,12 +1089,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_tiles_kernel(AttnArgs
         }
       c = logit_factor(a.scale, a.cache.amax[0], e);
     }
-    const int64_t pos = static_cast<int64_t>(rq.kv) - rq.n + qi;
-    int see_lo = 0, see_hi = rq.kv;
-    if (a.causal && pos + 1 < see_hi) see_hi = pos < 0 ? 0 : static_cast<int>(pos + 1);
-    if (a.window && pos - a.window + 1 > 0) see_lo = static_cast<int>(pos - a.window + 1);
-
-    float m = -INFINITY, l = 0.0f;
+    float m = -INFINITY, l;
+    const Keys see = see_of(a, rq, qi, &l);
     f32x16 o[DT];
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -1120,8 +1129,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_tiles_kernel(AttnArgs
 
     // Every load below is unconditional, from a place that is there: a wait for
     // one then leaves the later ones in flight, and nothing is waited for where
-    // it is loaded.  Past the table's row the last entry is read, for an id
-    // outside the cache page 0; neither is used (see decode).
+    // it is loaded.  Past the table's row, where no key is seen, the last entry
+    // is read, for an id outside the cache page 0; neither is used.
     const int32_t* ids_from = a.table_width > 0 ? row_table : a.cu_q;
     const int last_col = a.table_width > 0 ? static_cast<int>(a.table_width) - 1 : 0;
     const int in_page = (1 << shift) - 1;
@@ -1135,14 +1144,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_tiles_kernel(AttnArgs
     bool bad0, bad1;  // the page is not there
     const int64_t page_stride = a.cache.kv_heads * record;
     const uint8_t* data = a.cache.data + head * record;
-    auto record_of = [&](int32_t id, int key, bool* bad) -> const uint8_t* {
-      const bool out = static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.cache.pages);
-      *bad = out || (key >> shift) >= a.table_width;
-      return data + static_cast<int64_t>(out ? 0 : id) * page_stride;
+    auto record_of = [&](int32_t id, bool* bad) -> const uint8_t* {
+      *bad = static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.cache.pages);
+      return data + static_cast<int64_t>(*bad ? 0 : id) * page_stride;
     };
     auto load_raw = [&](int t) {
       const int key = t * Sh::BN + tok;
-      const uint8_t* rec = record_of(id0, key, &bad0);
+      const uint8_t* rec = record_of(id0, &bad0);
       const uint32_t at = key & in_page;
       const uint8_t* codes = rec + (code_at + at * (D / 2));
       const uint8_t* scales = rec + (scale_at + at * L);
@@ -1162,7 +1170,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_tiles_kernel(AttnArgs
         raw.w0 = *reinterpret_cast<const u32x4*>(codes);
         raw.s0 = *reinterpret_cast<const uint16_t*>(scales);
         const int key1 = key + kApart;
-        rec = record_of(id1, key1, &bad1);
+        rec = record_of(id1, &bad1);
         const uint32_t at1 = key1 & in_page;
         raw.w1 = *reinterpret_cast<const u32x4*>(rec + (code_at + at1 * (D / 2)));
         raw.s1 = *reinterpret_cast<const uint16_t*>(rec + (scale_at + at1 * L));
@@ -1250,7 +1258,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_tiles_kernel(AttnArgs
         }
         __builtin_amdgcn_sched_group_barrier(0x008, 4 * NQ, 0);
         if (key0 < inner.lo || key0 + 32 * SU > inner.hi) {
-          const int lo = see_lo - key0 - 8 * half, hi = see_hi - key0 - 8 * half;
+          const int lo = see.lo - key0 - 8 * half, hi = see.hi - key0 - 8 * half;
 #pragma unroll
           for (int u = 0; u < SU; ++u)
 #pragma unroll

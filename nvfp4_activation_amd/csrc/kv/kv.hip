@@ -361,8 +361,10 @@ nvfp4_status attention(const T* q, int64_t tokens, int32_t q_heads, const int64_
   }
   if (need > 0 && spans_meet(so, work)) return NVFP4_ERR_ARG;
   const int group = q_heads / cache->kv_heads;
+  const int64_t reach = batch->table_width * cache->page_size;
   AttnArgs<T> a{q, out, q_strides[0], q_strides[1], out_strides[0], out_strides[1], view_of(cache),
                 batch->table, batch->cu_q, batch->kv_lens, batch->table_width,
+                static_cast<int32_t>(reach < kMostKeys ? reach : kMostKeys),
                 static_cast<int32_t>(tokens), static_cast<int32_t>(batch->requests), group,
                 batch->causal, batch->window, batch->scale, 0, static_cast<float*>(workspace), 0, 0, nullptr,
                 FastDiv::make(static_cast<uint32_t>(cache->kv_heads)), FastDiv::make(static_cast<uint32_t>(group)),
