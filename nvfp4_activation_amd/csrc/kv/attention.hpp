@@ -225,12 +225,13 @@ __device__ __forceinline__ float logit_factor(float scale, float amax, int e) {
 // quotient may be subnormal (l < 2^46), times 2^100, with `back` to take that
 // off the result, exactly, after everything else.  0 for a row without keys.
 struct OutScale {
-  float f, back;
+  float g, back;
+  __device__ __forceinline__ float over(float l) const { return l == 0.0f ? 0.0f : g / l; }
 };
-__device__ __forceinline__ OutScale out_scale(float amax, float l) {
+__device__ __forceinline__ OutScale out_scale(float amax) {
   const float g = global_scale(amax);
-  const bool small = g < 0x1p-60f;  // the same for every row
-  return OutScale{l == 0.0f ? 0.0f : (small ? g * 0x1p100f : g) / l, small ? 0x1p-100f : 1.0f};
+  const bool small = g < 0x1p-60f;
+  return OutScale{small ? g * 0x1p100f : g, small ? 0x1p-100f : 1.0f};
 }
 
 // Inclusive sum over the wave.
@@ -371,15 +372,15 @@ __device__ __forceinline__ bool deal_out(const AttnArgs<T>& a, int n, F tiles, i
 // Scales a block of an output row, rotates it back and writes it.
 template <typename T>
 __device__ __forceinline__ void write_block(const AttnArgs<T>& a, int row0, int head, int row, int block,
-                                            float z[16], OutScale f) {
+                                            float z[16], float f, float back) {
   const int oi = static_cast<int>(a.by_group.div(static_cast<uint32_t>(row)));
   const int oh = head * a.group + (row - oi * a.group);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] *= f.f;
+  for (int i = 0; i < 16; ++i) z[i] *= f;
   if (a.cache.rotate) rotate16_block(z);
-  if (f.back != 1.0f) {
+  if (back != 1.0f) {  // the same for every row
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] *= f.back;
+    for (int i = 0; i < 16; ++i) z[i] *= back;
   }
   store16(a.out + static_cast<int64_t>(row0 + oi) * a.o_token + oh * a.o_head + block * 16, z);
 }
@@ -856,7 +857,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, rows_waves(sizeof(T) == 4, D, RT))
             a.part[a.part_ml + 2 * slot + 1] = ll;
           }
         } else {
-          write_block(a, rq.row0, head, orow, b, z, out_scale(a.cache.amax[1], ll));
+          const OutScale gv = out_scale(a.cache.amax[1]);
+          write_block(a, rq.row0, head, orow, b, z, gv.over(ll), gv.back);
         }
       }
       __syncthreads();  // the next rows write the merge buffers again
@@ -1352,7 +1354,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_tiles_kernel(AttnArgs
         a.part[a.part_ml + 2 * slot] = m;
         a.part[a.part_ml + 2 * slot + 1] = l;
       }
-      const OutScale f = out_scale(a.cache.amax[1], l);
+      const OutScale gv = out_scale(a.cache.amax[1]);
+      const float f = gv.over(l);
       // element 8 c + j, c = 8 ga + 4 half + b, is in o[j / JW][4 (ga + GA (j % JW)) + b]
 #pragma unroll
       for (int ga = 0; ga < Sh::GA; ++ga)
@@ -1368,7 +1371,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void kv_attn_tiles_kernel(AttnArgs
           if (!whole)
             store16(a.part + slot * D + block * 16, z);
           else
-            write_block(a, rq.row0, head, row, block, z, f);
+            write_block(a, rq.row0, head, row, block, z, f, gv.back);
         }
     }
     at += here;
@@ -1417,6 +1420,7 @@ __device__ __forceinline__ void join_row(const AttnArgs<T>& a, const JoinPart& p
   float z[16], ll = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  const OutScale gv = out_scale(a.cache.amax[1]);
   for (int s = s0; s < n; s += 32) {
     if (s != s0) fetch(s);
 #pragma unroll
@@ -1439,7 +1443,7 @@ __device__ __forceinline__ void join_row(const AttnArgs<T>& a, const JoinPart& p
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i] += __shfl_xor(z[i], d);
   }
-  if (s0 == 0) write_block(a, row0, head, row, b, z, out_scale(a.cache.amax[1], ll));
+  if (s0 == 0) write_block(a, row0, head, row, b, z, gv.over(ll), gv.back);
 }
 
 // Workgroups (w, .) join the unit that workgroup w's range of tiles begins
@@ -1462,6 +1466,7 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs<T> a, JoinPa
   if (n <= 4) {
     // a lane a block of a row, which sums its parts by itself
     constexpr int L = D / 16;
+    const OutScale gv = out_scale(a.cache.amax[1]);
     const float2* ml = reinterpret_cast<const float2*>(p.part + p.part_ml);
     for (int i = 256 * blockIdx.y + threadIdx.x; i < count * L; i += 256 * gridDim.y) {
       const int r = i / L, b = i % L;
@@ -1494,7 +1499,7 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs<T> a, JoinPa
           z[4 * k + 3] = __builtin_fmaf(f, v[s][k].w, z[4 * k + 3]);
         }
       }
-      write_block(a, u.row0, u.head, u.base + r, b, z, out_scale(a.cache.amax[1], ll));
+      write_block(a, u.row0, u.head, u.base + r, b, z, gv.over(ll), gv.back);
     }
     return;
   }
