@@ -440,7 +440,9 @@ nvfp4_status nvfp4_kv_append_f32(const float *k, const float *v, int64_t tokens,
  *              as 0.
  *   max_q, max_kv  upper estimates of n and kv_len, >= 0.  They shape the
  *              launch (with the workspace's size) and no more: results are
- *              right for every value.
+ *              right for every value.  max_q is worth knowing: one token each
+ *              of 64 requests of up to 8192 keys takes 80 us with max_q 1 and
+ *              110 us with max_q 64, the number of all tokens.
  *   causal     0 or 1; window  0 (none), or > 0 with causal == 1.
  *   scale      finite and > 0.
  */
@@ -465,7 +467,8 @@ typedef struct nvfp4_kv_batch {
  * Rounding: bf16 takes the rotated queries (times a power of two for each
  * row) and the softmax weights in fp16 (2^-11 relative), sums in binary32 and
  * rounds once to bf16; f32 takes both as the sum of two fp16 numbers, which
- * keeps 22 bits.  Decoded values E2M1 * E4M3 are exact in fp16.  Logits are to
+ * keeps 22 bits.  Weights below 2^-26 (bf16) or 2^-14 (f32) of the row's
+ * largest are off by up to 2^-37 of that one instead.  Decoded values E2M1 * E4M3 are exact in fp16.  Logits are to
  * stay in binary32's range.
  * The same arguments give the same bits; with other requests beside it, or other
  * estimates, a request's sums may be split elsewhere and round differently.

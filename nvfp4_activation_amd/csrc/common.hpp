@@ -9,7 +9,7 @@
 #include "nvfp4rq_device.hpp"
 
 namespace nvfp4rq {
-namespace {  // one translation unit (nvfp4rq.hip): internal linkage
+namespace {  // internal linkage: nvfp4rq.hip and kv/kv.hip each have their own
 
 constexpr int kThreads = 256;      // 4 waves of 64
 // 16-byte pieces per lane per iteration in the bf16 amax pass: 4 KiB per

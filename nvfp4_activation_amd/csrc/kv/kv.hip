@@ -211,8 +211,14 @@ nvfp4_status plan_attention(int64_t tokens, int32_t q_heads, const nvfp4_kv_cach
   // 256 rows, and of 128 rows over 4k keys 288 us and 249 us.  At head_dim 256,
   // where a tile has 128 rows, they are 128: 657 us and 1027 us over 4k keys,
   // and with 256 rows 335 us and 266 us.  Twice as many are few where all units
-  // of the call run at once, two a compute unit: 7 requests of 99 rows in a
-  // window of 1024 keys take 22 us and 50 us.
+  // of the call run at once, two a compute unit.  Over 2048 and 8192 keys, in
+  // us on the rows kernel and on the tiles kernel: 16 requests of 128 rows on 8
+  // heads of 128 (512 units) 40 and 59, 132 and 153, 17 of them 56 and 50, 172
+  // and 152, a single one 24 and 35, 43 and 42; fp32 on 5 heads of 64, 25
+  // requests of 126 rows (500 units) 38 and 45, 132 and 131, 26 of them 54 and
+  // 45, 174 and 124.  At head_dim 256 the limit comes early for short keys: 32
+  // requests of 256 rows on one head 44 and 101, 157 and 208, 33 of them 61 and
+  // 93, 199 and 191.
   const int64_t forced = kv_env_int("NVFP4RQ_KV_FEW_ROWS");
   int64_t few = forced ? forced : c->head_dim == 256 ? 128 : 64;
   const int64_t unit_rows = 16 * most_row_tiles(c->head_dim);
@@ -231,7 +237,17 @@ nvfp4_status plan_attention(int64_t tokens, int32_t q_heads, const nvfp4_kv_cach
   // would have too little.  With 8 heads of 128, one token a request, in us
   // whole and in ranges: 1 request over 776 keys 16 and 20, over 2000 17 and
   // 21, over 5000 33 and 20; 32 over 3000 keys 24 and 33; 64 over 3000 keys 40
-  // and 54, over 8191 106 and 118; 256 over up to 4000 146 and 164.
+  // and 54; 256 over up to 4000 146 and 164.  About the limits, with 8 query
+  // heads a key head and 768 resident workgroups: 8 and 16 requests (no third)
+  // over 2048 keys 17 and 21, 16 and 20, over 4096 27 and 23, 27 and 34; 31 and
+  // 32 requests (a third from 32 on) over 4096 29 and 41, 30 and 41, over 8192
+  // 56 and 63, 56 and 65; 63, 64 and 65 requests (two thirds from 64 on) over
+  // 8192 98 and 114, 102 and 117, 128 and 115.  Where the lengths are between a
+  // quarter of that and all of it: 32 requests over 8192 51 and 49, 63, 64 and
+  // 65 over 8192 79 and 78, 78 and 79, 95 and 81.  So the limits sit where
+  // ragged lengths break even; equal lengths whose units fill the same number
+  // of rounds of the compute units would gain some 15% by staying whole past
+  // them, and one unit over such a number loses as much.
   const int64_t keys = b->window > 0 && b->max_kv > b->window + max_q ? b->window + max_q : b->max_kv;
   p->rows = AttnLaunch{p->few > 0, true, kv_env_int("NVFP4RQ_KV_ROWS_WGS"), 0};
   if (p->rows.wgs == 0) {

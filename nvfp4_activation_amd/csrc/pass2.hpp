@@ -11,7 +11,7 @@
 #include "common.hpp"
 
 namespace nvfp4rq {
-namespace {  // one translation unit (nvfp4rq.hip): internal linkage
+namespace {  // internal linkage: nvfp4rq.hip and kv/kv.hip each have their own
 
 // Where block b's scale byte is stored.  Row-major: byte b of the
 // [rows, cols/16] matrix.  Swizzled (the tiled layout GEMMs read, page "A

@@ -5,8 +5,9 @@ what each computes and how a record is laid out.  A step of a server:
 
     plan = kv_plan(cached, added, table, free, head, page_size, tokens)
     kv_append(k, v, plan.slots, cache, amax)
-    out = kv_attention(q, cache, amax, table, plan.cu_q, plan.kv_lens)
+    out = kv_attention(q, cache, amax, table, plan.cu_q, plan.kv_lens, max_q=most)
 
+with ``most`` the most tokens that any request of the step adds.
 ``cache`` is a uint8 tensor [pages, kv_heads, page bytes] (kv_cache makes
 one); its page size follows from the head dimension of k or q.  ``amax`` holds
 the maxima of rotated K and V that fix the two global scales, for instance
@@ -272,9 +273,11 @@ def kv_attention(q: torch.Tensor, cache: torch.Tensor, amax: torch.Tensor, table
     float32 [tokens, q_heads, head_dim]; request r's rows are cu_q[r] ..
     cu_q[r + 1] - 1 and its keys the first kv_lens[r] tokens of table[r], its new
     ones included.  max_q and max_kv: the most of either that any request has
-    (bounds from the shapes when None); they shape the launch, not the result.
+    (bounds from the shapes when None: all tokens, the table's width); they shape
+    the launch, not the result.  Give max_q where single tokens of many requests
+    come together: 64 of them over 8192 keys take 80 us with it and 110 without.
     scale: head_dim ** -0.5 when None.  Rows in no request are left as they were
-    in out.  workspace: a uint8 tensor of kv_attention_workspace bytes, allocated
+    in out, and hold anything, NaN included, where out is None.  workspace: a uint8 tensor of kv_attention_workspace bytes, allocated
     when None; calls that share one must be ordered.  No gradients: a backward
     pass that reaches the result raises, unless it was written to the caller's
     out, which keeps no record of q."""
