@@ -213,17 +213,19 @@ __device__ __forceinline__ int row_exponent(float top) {
 // Significands and exponents apart: however small g or the scale, what the
 // other or the query's 2^e makes up for keeps its bits.  Not 0, so that a
 // masked logit stays -inf (|s| < 2^34: nothing is lost), and not infinite, so
-// that a logit of 0 stays 0.
+// that a logit of 0 stays 0.  NaN where the maximum is none: results then show
+// it.
 __device__ __forceinline__ float logit_factor(float scale, float amax, int e) {
   const float g = global_scale(amax);
   const float f = __builtin_amdgcn_frexp_mantf(scale) * kLog2e * __builtin_amdgcn_frexp_mantf(g);
   const int x = __builtin_amdgcn_frexp_expf(scale) + __builtin_amdgcn_frexp_expf(g) - e;
-  return __builtin_amdgcn_fmed3f(__builtin_ldexpf(f, x), 0x1p-126f, 0x1.fffffep127f);
+  constexpr float kMost = 0x1.fffffep127f;
+  return g <= kMost ? __builtin_amdgcn_fmed3f(__builtin_ldexpf(f, x), 0x1p-126f, kMost) : NAN;
 }
 
 // What brings a row's sums to its result, g / l: where g is so small that the
 // quotient may be subnormal (l < 2^46), times 2^100, with `back` to take that
-// off the result, exactly, after everything else.  0 for a row without keys.
+// off the result after everything else.  0 for a row without keys.
 struct OutScale {
   float g, back;
   __device__ __forceinline__ float over(float l) const { return l == 0.0f ? 0.0f : g / l; }

@@ -112,3 +112,13 @@ def test_append_with_extreme_maxima(nv, amax, dtype):  # noqa: F811
     want = np.zeros((3, 2, kv_model.page_bytes(16, 128)), np.uint8)
     kv_model.append(k, v, list(range(40)), want, a, 16)
     assert np.array_equal(cache.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_maxima_that_are_not_finite_show(nv, path, dtype, bad):  # noqa: F811
+    """A maximum that is no number leaves no ordinary results."""
+    say("not finite", path, dtype, bad)
+    s = scene(dtype, 128)
+    assert run(nv, s, s.q, np.array([bad, 9.0], np.float32), None).isnan().all()
+    assert not run(nv, s, s.q, np.array([4.0, bad], np.float32), None).isfinite().any()
