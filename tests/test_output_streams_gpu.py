@@ -113,3 +113,46 @@ def test_memory_in_use_on_the_current_stream_stays(nv):
         assert other.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(seen, kv_attention(nv, tokens=48))
+
+
+def test_captured_calls_on_a_forked_stream(nv):
+    """A step captured with its calls on a stream that forks off and joins, the
+    outputs allocated by the calls; replayed with eager work between."""
+    say("capture")
+    gen = torch.Generator().manual_seed(9)
+    cache = nv.kv_cache(8, 2, 64, 16)
+    amax, table = torch.full((2,), 4.0, device=DEV), torch.full((2, 4), -1, dtype=torch.int32, device=DEV)
+    free, head = i32(list(range(8))), i32([0])
+    cached, added = i32([0, 0]), i32([20, 3])
+    q, k, v = (torch.randn(32, h, 64, generator=gen).to(DEV) for h in (4, 2, 2))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def step(stream):
+        p = nv.kv_plan(cached, added, table, free, head, 16, 32, stream=stream)
+        nv.kv_append(k, v, p.slots, cache, amax, stream=stream)
+        codes = nv.rotquant(q.view(32, 256), stream=stream)
+        return nv.kv_attention(q, cache, amax, table, p.cu_q, p.kv_lens, max_kv=1 << 20, stream=stream), p, codes
+
+    want, plan, codes = step(None)
+    torch.cuda.synchronize()
+    want = want[:23].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out, p, c = step(side)
+        dropped = step(side)[0]  # one whose memory is free again before the end
+        del dropped
+        torch.cuda.current_stream().wait_stream(side)
+    for rep in range(4):
+        say("replay", rep)
+        cache.zero_()
+        table.fill_(-1)
+        out.fill_(7.0)
+        graph.replay()
+        side.wait_stream(torch.cuda.current_stream())
+        eager = step(side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        assert torch.equal(out[:23], want) and torch.equal(eager[0][:23], want)
+        assert torch.equal(p.slots, plan.slots) and all(torch.equal(a, b) for a, b in zip(c, codes))
