@@ -277,10 +277,11 @@ def kv_attention(q: torch.Tensor, cache: torch.Tensor, amax: torch.Tensor, table
     the launch, not the result.  Give max_q where single tokens of many requests
     come together: 64 of them over 8192 keys take 80 us with it and 110 without.
     scale: head_dim ** -0.5 when None.  Rows in no request are left as they were
-    in out, and hold anything, NaN included, where out is None.  workspace: a uint8 tensor of kv_attention_workspace bytes, allocated
-    when None; calls that share one must be ordered.  No gradients: a backward
-    pass that reaches the result raises, unless it was written to the caller's
-    out, which keeps no record of q."""
+    in out, and hold anything, NaN included, where out is None.  workspace: a
+    uint8 tensor of kv_attention_workspace bytes, allocated when None; calls that
+    share one must be ordered.  No gradients: a backward pass that reaches the
+    result raises, unless it was written to the caller's out, which keeps no
+    record of q."""
     if out is None and torch.is_grad_enabled() and isinstance(q, torch.Tensor) and q.requires_grad:
         return _NoGradient.apply(q, lambda: kv_attention(
             q.detach(), cache, amax, table, cu_q, kv_lens, max_q, max_kv, causal, window, scale, rotate, None,
